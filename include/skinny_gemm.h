@@ -461,7 +461,8 @@ SG_API int kv_read_nvfp4(const void *cache, int64_t num_pages, int64_t page_pitc
  * Q and O: `tokens` rows of heads * 128 bf16, pitches ldq and ldo.  Scores, softmax
  * and sums are fp32; keys and values enter the products exactly (a code times its
  * scale has at most 6 significant bits).  A value that is NaN reaches only queries
- * that see it.  Results are the same on every run.
+ * that see it; a query head with a NaN or an infinity that sees a key gives NaN.
+ * Results are the same on every run.
  *
  * A request whose lengths contradict the call (negative, more than max_q queries,
  * more keys than max_pages * page_size, rows outside [0, tokens)) is not computed,

@@ -576,10 +576,13 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) kv_stream_kernel(const K
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
         const int e = top == 0 ? 0 : max(-100, min(100, static_cast<int>(top >> 7) - 127));
-        // the scale's sign goes into Q; with scale 0 every score is 0 (a NaN or infinity
-        // in Q still makes its row NaN)
-        const float shift = exp2f(static_cast<float>(13 - e)) *
-                            (p.scale_log2 < 0.f ? -1.f : p.scale_log2 == 0.f ? 0.f : 1.f);
+        // The scale's sign goes into Q; with scale 0 every score is 0.  A row with a NaN or
+        // an infinity becomes NaN as a whole: its scores are NaN or infinite whatever the
+        // key, and a softmax over any of those is NaN (left as they are, infinities of one
+        // sign would all be -inf and pass for masked keys).
+        const float shift = top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
+                                           : exp2f(static_cast<float>(13 - e)) *
+                                                 (p.scale_log2 < 0.f ? -1.f : p.scale_log2 == 0.f ? 0.f : 1.f);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           qf[nt][i] = half2_bits(__floats2half2_rn(__uint_as_float(w[i] << 16) * shift,

@@ -746,8 +746,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefill_kernel(const KvAttnP
                              max(v[i].y & 0x7FFFu, (v[i].y >> 16) & 0x7FFFu));
           top = __reduce_max_sync(0xFFFFFFFFu, top);
           const int e = top == 0 ? 0 : max(-100, min(100, static_cast<int>(top >> 7) - 127));
-          // the scale's sign goes into Q; with scale 0 every score is 0
-          const float up = __int_as_float((127 + 13 - e) << 23) * sign;  // 2^(13 - e)
+          // 2^(13 - e) and the scale's sign (with scale 0 every score is 0); a row with a NaN
+          // or an infinity becomes NaN as a whole, as its softmax is (infinite scores of one
+          // sign would all be -inf and pass for masked keys)
+          const float up = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : __int_as_float((127 + 13 - e) << 23) * sign;
           const uint32_t lo = h2_bits(
               __floats2half2_rn(__uint_as_float(v[i].x << 16) * up, __uint_as_float(v[i].x & 0xFFFF0000u) * up));
           const uint32_t hi = h2_bits(

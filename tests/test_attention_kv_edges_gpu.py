@@ -1,0 +1,73 @@
+"""Attention over the paged NVFP4 cache at the edges of its inputs, on both kernels:
+infinite queries, queries and scales far from 1, counts at the ends of their types,
+weights whose larger partners meet zero values, the automatic choice of the kernel,
+and a data error beside a timeout.
+
+Tolerance as in test_attention_kv_gpu.py, with the weights' term by the kernel that
+runs: fp16 weights on the streaming kernel (half a step is 2^-11), bf16 on the tcgen05
+kernel (2^-8)."""
+import numpy as np
+import pytest
+
+import oracle  # noqa: F401
+import synthetic as syn
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import skinny_gemv_gb300 as sg  # noqa: E402
+from test_attention_kv_gpu import D, PATHS, Case, clean, dev, f64, i32  # noqa: E402
+
+ONES = 6 * 11 / 64  # what a block of ones reads back as: scale 11 / 64, code 6
+
+
+def fill(c, k=None, v=None):
+    """Writes K and V (float, [tokens, kv_heads, D], tokens of all requests one after
+    another; None: ones) over the rows of a Case's cache."""
+    rows = np.concatenate([np.arange(n) for n in c.lens]).astype(int)
+    owner = np.repeat(np.arange(len(c.lens)), c.lens)
+    slots = c.table[owner, rows // c.page] * c.page + rows % c.page
+    one = np.ones((len(rows), c.kv_heads, D))
+    k, v = (dev(syn.f64_to_bf16_bits(one if x is None else x)) for x in (k, v))
+    sg.kv_append_nvfp4(k, v, c.view(), i32(slots), c.page, c.k_scale, c.v_scale)
+    c.host = c.cache.cpu().numpy()
+
+
+def check(c, path, causal=True, scale=None, auto=None):
+    """Against the oracle, with the weights' bound of the kernel `path` (`auto`: run
+    SG_PATH_AUTO, which takes that kernel)."""
+    got = f64(c.run(causal, scale, path=sg.PATH_AUTO if auto else path))
+    clean()
+    ref, W = c.ref(causal, scale)
+    weights = 2.0 ** (-11 if path == sg.PATH_STREAM else -8)
+    assert np.isfinite(got).all()
+    bound = 2.0 ** -8 * np.abs(ref) + weights * (W + np.abs(ref)) + 2.0 ** -12 * W
+    d = np.abs(got - ref)
+    assert (d <= bound).all(), (d - bound).max()
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("scale", [None, -0.1, 0.0])
+def test_infinite_queries_give_nan(path, value, scale):
+    """Keys of one sign: every score of the row is an infinity of one sign, and a softmax
+    of those is NaN, not a row that sees nothing.  Rows that see no key stay 0."""
+    for q_lens, lens in (([1], [1]), ([1, 3], [200, 40]), ([50, 9], [600, 4]), ([200], [500])):
+        c = Case(q_lens, lens, 8, 2, 16)
+        fill(c, v=np.random.default_rng(1).standard_normal((sum(lens), 2, D)))
+        ref = c.run(scale=scale, path=path).clone()
+        q = dev(c.Q).clone()
+        rows = [0, q_lens[0] - 1, int(c.cu[-1]) - 1]
+        for t in rows:
+            q[t, 6, 9] = value
+        got = c.run(scale=scale, Q=q, path=path)
+        clean()
+        keep = torch.ones(got.shape[:2], dtype=torch.bool)
+        keep[rows, 6] = False
+        assert torch.equal(got[keep], ref[keep])
+        for t in rows:
+            assert torch.isnan(got[t, 6]).all(), t
+        if lens[-1] < q_lens[-1]:  # the first of the last request's queries is blind
+            t = int(c.cu[-2])
+            q[t, 6, 9] = value
+            assert (c.run(scale=scale, Q=q, path=path)[t] == 0).all()
