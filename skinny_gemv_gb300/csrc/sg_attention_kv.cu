@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) kv_stream_kernel(const K
         for (int i = 0; i < 16; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        const int e = top == 0 ? 0 : max(-100, min(100, static_cast<int>(top >> 7) - 127));
+        const int e = top == 0 ? 0 : max(-100, min(127, static_cast<int>(top >> 7) - 127));
         // The scale's sign goes into Q; with scale 0 every score is 0.  A row with a NaN or
         // an infinity becomes NaN as a whole: its scores are NaN or infinite whatever the
         // key, and a softmax over any of those is NaN (left as they are, infinities of one
@@ -587,7 +587,9 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) kv_stream_kernel(const K
         for (int i = 0; i < 16; ++i)
           qf[nt][i] = half2_bits(__floats2half2_rn(__uint_as_float(w[i] << 16) * shift,
                                                    __uint_as_float(w[i] & 0xFFFF0000u) * shift));
-        const float back = p.scale_log2 == 0.f ? 1.f : exp2f(static_cast<float>(e - 13)) * fabsf(p.scale_log2);
+        // (at least 2^-126: an underflow to 0 would turn masked scores, -inf, into NaN)
+        const float back =
+            p.scale_log2 == 0.f ? 1.f : fmaxf(exp2f(static_cast<float>(e - 13)) * fabsf(p.scale_log2), 0x1p-126f);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int r2 = 8 * nt + 2 * t4 + c;

@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefill_kernel(const KvAttnP
           uint32_t top = max(max(v[i].x & 0x7FFFu, (v[i].x >> 16) & 0x7FFFu),
                              max(v[i].y & 0x7FFFu, (v[i].y >> 16) & 0x7FFFu));
           top = __reduce_max_sync(0xFFFFFFFFu, top);
-          const int e = top == 0 ? 0 : max(-100, min(100, static_cast<int>(top >> 7) - 127));
+          const int e = top == 0 ? 0 : max(-100, min(127, static_cast<int>(top >> 7) - 127));
           // 2^(13 - e) and the scale's sign (with scale 0 every score is 0); a row with a NaN
           // or an infinity becomes NaN as a whole, as its softmax is (infinite scores of one
           // sign would all be -inf and pass for masked keys)
@@ -757,7 +757,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefill_kernel(const KvAttnP
           const int chunk = (lane / 2) & 7;
           uint8_t* box = smem + kPfQOff + (2 * (r / kPfTileRows) + lane / 16) * kPfBox + (r % kPfTileRows) * 128;
           *reinterpret_cast<uint2*>(box + ((chunk ^ (r & 7)) * 16) + (lane & 1) * 8) = make_uint2(lo, hi);
-          if (lane == 0) row_scale[r] = sign == 0.f ? 1.f : __int_as_float((127 - 13 + e) << 23) * fabsf(p.scale_log2);
+          // (at least 2^-126: an underflow to 0 would turn masked scores, -inf, into NaN)
+          if (lane == 0)
+            row_scale[r] =
+                sign == 0.f ? 1.f : fmaxf(__int_as_float((127 - 13 + e) << 23) * fabsf(p.scale_log2), 0x1p-126f);
         }
       }
       fence_proxy_async_smem();

@@ -71,3 +71,27 @@ def test_infinite_queries_give_nan(path, value, scale):
             t = int(c.cu[-2])
             q[t, 6, 9] = value
             assert (c.run(scale=scale, Q=q, path=path)[t] == 0).all()
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("power", [115, 60, -100])
+def test_powers_of_two_move_between_queries_and_scale(path, power):
+    """Queries times 2^power with the scale times 2^-power: the same scores, the same bits."""
+    for q_lens, lens in (([1, 3], [300, 70]), ([90], [200])):
+        c = Case(q_lens, lens, 8, 2, 16)
+        # magnitudes of at least 1, so that no element becomes subnormal
+        c.Q = syn.f64_to_bf16_bits(np.sign(f64(dev(c.Q))) * np.maximum(np.abs(f64(dev(c.Q))), 1.0))
+        want = c.run(scale=2.0 ** -4, path=path).clone()
+        c.Q = syn.f64_to_bf16_bits(f64(dev(c.Q)) * 2.0 ** power)
+        assert torch.equal(c.run(scale=2.0 ** (-4 - power), path=path), want)
+        clean()
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_vanishing_scores_leave_masked_keys_masked(path):
+    """Queries and scale so small that their product underflows: all visible keys weigh
+    the same, and a masked one nothing (not 0 * infinity)."""
+    for q_lens, lens in (([1], [37]), ([5], [5]), ([100], [150])):
+        c = Case(q_lens, lens, 4, 2, 16)
+        c.Q = syn.f64_to_bf16_bits(f64(dev(c.Q)) * 2.0 ** -115)
+        check(c, path, scale=1e-30)
