@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) kv_stream_kernel(const K
             const uint32_t ok2 = (ok >> (2 * half_step)) & 3u;
             float x[2][NT][4];
             scores<NT>(st, lane, qf, x);
-            const bool tail = ok2 != 3u || key0 + 32 > lim_min;
+            const bool tail = ok2 != 3u || key0 > lim_min - 32;  // (key0 + 32 may pass 2^31)
             if (tail) {
 #pragma unroll
               for (int tl = 0; tl < 2; ++tl)

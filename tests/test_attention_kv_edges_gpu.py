@@ -95,3 +95,21 @@ def test_vanishing_scores_leave_masked_keys_masked(path):
         c = Case(q_lens, lens, 4, 2, 16)
         c.Q = syn.f64_to_bf16_bits(f64(dev(c.Q)) * 2.0 ** -115)
         check(c, path, scale=1e-30)
+
+
+def test_the_longest_sequence_ends_where_it_says():
+    """2^31 - 1 keys, the last page entry's last token past the end: its values are NaN
+    and must stay unseen.  (One page serves as all the others: 19 MB of cache.)"""
+    page = 65536
+    cache = torch.empty(2, sg.kv_nvfp4_page_bytes(1, page), dtype=torch.uint8, device="cuda")
+    ones = torch.ones(2 * page, 1, D, dtype=torch.bfloat16, device="cuda")
+    v = ones.clone()
+    v[-1] = float("nan")
+    sg.kv_append_nvfp4(ones, v, cache, torch.arange(2 * page, dtype=torch.int32, device="cuda"), page)
+    table = torch.zeros(1, 32768, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    for heads in (1, 16):  # 8 and 16 query rows per unit of the streaming kernel
+        q = torch.zeros(1, heads, D, dtype=torch.bfloat16, device="cuda")
+        out = sg.attention_kv_nvfp4(q, cache, table, i32([2 ** 31 - 1]), i32([0, 1]), 1, page, 1, path=sg.PATH_STREAM)
+        clean()
+        assert (out == ONES).all()
