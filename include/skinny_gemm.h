@@ -469,8 +469,9 @@ SG_API int kv_read_nvfp4(const void *cache, int64_t num_pages, int64_t page_pitc
  * and keys on a page id outside the cache are treated as masked
  * (SG_ERR_BAD_INDEX later, in both cases).
  *
- * Requirements and errors as for the calls above; scale finite.  batch, tokens,
- * max_q or heads = 0: no work.
+ * Requirements and errors as for the calls above; scale finite; tokens and
+ * max_pages below 2^31, batch and min(max_q, tokens) * heads below 2^31 - 1024.
+ * batch, tokens, max_q or heads = 0: no work.
  */
 SG_API int attention_kv_nvfp4(const void *Q, const void *cache, void *O, const int32_t *block_table,
                               int64_t table_pitch, int64_t max_pages, const int32_t *seq_lens, const int32_t *cu_q,

@@ -862,6 +862,7 @@ int run_attention(DeviceState& d, int dev, const void* Q, const void* K, const v
 constexpr int64_t kKvMaxPageSize = 65536;
 constexpr int64_t kRopeMaxDim = 512;       // 32 lanes of 16 elements
 constexpr int64_t kPagesRowsPerCta = 4096;
+constexpr int64_t kKvMaxIndex = INT32_MAX - 1024;
 
 // A cache scale: a power of two (so that quantisation stays exact), 2^-32 .. 2^32.
 bool kv_scale_ok(float g) {
@@ -1345,7 +1346,9 @@ int attention_kv_nvfp4_path(const void* Q, const void* cache, void* O, const int
   if (batch > INT32_MAX || tokens > INT32_MAX || heads > INT32_MAX / kKvDim || max_pages > INT32_MAX)
     return SG_ERR_INVALID_ARG;
   max_q = std::min(max_q, tokens);
-  if (batch * max_q > INT32_MAX / heads) return SG_ERR_INVALID_ARG;  // grid sizes in int32
+  // int32 in the kernels: a request's query rows, and the requests, each up to a multiple
+  // of the CTA's; sums over requests are int64
+  if (max_q > kKvMaxIndex / heads || batch > kKvMaxIndex) return SG_ERR_INVALID_ARG;
   const int geo = kv_check_cache(cache, num_pages, page_pitch, page_size, kv_heads);
   if (geo != SG_OK) return geo;
   if (!Q || !O || !seq_lens || !cu_q || (max_pages > 0 && !block_table) || ldq < heads * head_dim ||

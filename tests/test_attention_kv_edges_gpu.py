@@ -113,3 +113,29 @@ def test_the_longest_sequence_ends_where_it_says():
         out = sg.attention_kv_nvfp4(q, cache, table, i32([2 ** 31 - 1]), i32([0, 1]), 1, page, 1, path=sg.PATH_STREAM)
         clean()
         assert (out == ONES).all()
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_a_long_chunk_beside_thousands_of_decode_requests(path):
+    """batch * max_q * heads past 2^31; sampled rows against the oracle, a row of the
+    chunk as a single query over the keys it sees."""
+    rng = np.random.default_rng(3)
+    n, chunk, heads = 4097, 4097, 128
+    at = 1000
+    q_lens = [1] * n
+    q_lens[at] = chunk
+    lens = [int(x) for x in rng.integers(1, 30, n)]
+    lens[at] = chunk
+    assert n * chunk * heads >= 2 ** 31
+    c = Case(q_lens, lens, heads, 8, 16)
+    got = f64(c.run(path=path))
+    clean()
+    assert np.isfinite(got).all()
+    reqs = np.concatenate([rng.choice(n, 40, replace=False), np.full(4, at)])
+    tokens = np.where(reqs == at, rng.integers(0, chunk, len(reqs)), 0)
+    rows = c.cu[reqs] + tokens
+    sees = np.where(reqs == at, tokens + 1, np.array(lens)[reqs])
+    ref, W = oracle.attention_kv(c.Q[rows], c.host, c.table[reqs], sees, np.arange(len(rows) + 1), 8, 16, True, None,
+                                 c.k_scale, c.v_scale)
+    bound = 2.0 ** -8 * np.abs(ref) + 2.0 ** (-11 if path == sg.PATH_STREAM else -8) * (W + np.abs(ref)) + 2.0 ** -12 * W
+    assert (np.abs(got[rows] - ref) <= bound).all()
