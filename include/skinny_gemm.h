@@ -547,13 +547,14 @@ SG_API int sg_last_cuda_error(void);
 
 /*
  * sg_check_device_errors -- synchronises `stream`, then reads and clears the
- * current device's kernel error word.  Returns SG_OK, SG_ERR_TIMEOUT (a kernel
+ * current device's kernel error record.  Returns SG_OK, SG_ERR_TIMEOUT (a kernel
  * gave up on a bounded wait; its output is undefined and the workspace counters
  * are reset here so later calls are correct), SG_ERR_BAD_INDEX (a kernel of the
  * paged cache or the rotation met an index out of range and skipped it: code 16
  * slot, 17 page id, 18 position, 19 a request's lengths; `where` is the token row
- * or request), or SG_ERR_CUDA.  If `detail` is not
- * NULL it receives {code, block, warp, where} of the first recorded error.
+ * or request), or SG_ERR_CUDA.  If both kinds happened the timeout is returned and
+ * the bad index by the next call.  If `detail` is not NULL it receives {code, block,
+ * warp, where} of the first error recorded of the kind returned.
  */
 SG_API int sg_check_device_errors(sg_stream_t stream, uint32_t detail[4]);
 

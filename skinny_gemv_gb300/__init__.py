@@ -718,7 +718,8 @@ def set_wait_timeout_ns(ns: int) -> None:
 
 
 def check_device_errors(stream=None):
-    """Synchronises the stream; returns (status, detail[4]) of kernel wait timeouts."""
+    """Synchronises the stream; returns (status, detail[4]) of kernel wait timeouts and
+    indices out of range, a timeout first (the other kind by the next call)."""
     detail = (ctypes.c_uint32 * 4)()
     st = load().sg_check_device_errors(_stream_handle(stream), detail)
     return st, list(detail)

@@ -1,5 +1,5 @@
 // Host side of the C ABI declared in include/skinny_gemm.h: argument checks,
-// per-device state (properties, workspace, error word), tensor-map encoding,
+// per-device state (properties, workspace, error records), tensor-map encoding,
 // launch planning and dispatch.  Nothing here computes any part of C: every
 // output element is produced by the kernels.
 #include <cuda.h>
@@ -39,7 +39,7 @@ constexpr int64_t kCcMaxRowsPerCta = 256;
 struct DeviceState {
   bool props_ready = false;
   int sm_count = 0, cc_major = 0, cc_minor = 0, smem_optin = 0, l2_bytes = 0;
-  void* workspace = nullptr;  // [partials | counters | error word]
+  void* workspace = nullptr;  // [partials | counters | error records]
   float* partials = nullptr;
   uint32_t* counters = nullptr;
   DeviceError* err = nullptr;
@@ -1425,18 +1425,26 @@ int sg_check_device_errors(sg_stream_t stream, uint32_t detail[4]) {
   e = cudaMemcpyAsync(&h, d->err, sizeof h, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e);
-  if (h.code == 0) return SG_OK;
+  const bool waited = h.wait.code != 0;
+  const DeviceErrorRecord& r = waited ? h.wait : h.data;
+  if (r.code == 0) return SG_OK;
   if (detail) {
-    detail[0] = h.code;
-    detail[1] = h.block;
-    detail[2] = h.role;
-    detail[3] = h.where;
+    detail[0] = r.code;
+    detail[1] = r.block;
+    detail[2] = r.role;
+    detail[3] = r.where;
   }
-  // Clear the error word and every arrival counter an aborted launch may have left.
-  e = cudaMemsetAsync(d->counters, 0, kNumCounters * sizeof(uint32_t) + sizeof(DeviceError), s);
+  // Clear the record and, after a timeout, every arrival counter the aborted launch may
+  // have left.  A data error beside a timeout is kept for the next check.
+  if (waited) {
+    e = cudaMemsetAsync(d->counters, 0, kNumCounters * sizeof(uint32_t), s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(&d->err->wait, 0, sizeof r, s);
+  } else {
+    e = cudaMemsetAsync(&d->err->data, 0, sizeof r, s);
+  }
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e);
-  return h.code >= kDevFirstDataError ? SG_ERR_BAD_INDEX : SG_ERR_TIMEOUT;
+  return waited ? SG_ERR_TIMEOUT : SG_ERR_BAD_INDEX;
 }
 
 int sg_plan(int64_t M, int64_t N, int64_t K, int32_t num_sms, int32_t entry, sg_plan_info* out) {

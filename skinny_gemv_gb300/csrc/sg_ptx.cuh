@@ -12,7 +12,7 @@
 namespace sg {
 
 // ---------------------------------------------------------------------------
-// Error word written by kernels (one per device, in the library workspace).
+// Error records written by kernels (one block per device, in the library workspace).
 // ---------------------------------------------------------------------------
 enum DeviceErrorCode : uint32_t {
   kDevOk = 0,
@@ -30,11 +30,18 @@ enum DeviceErrorCode : uint32_t {
   kDevBadRequest = 19,       // a request's lengths contradict the call's bounds
 };
 
-struct DeviceError {
+struct DeviceErrorRecord {
   uint32_t code;   // first error seen (0 = none)
   uint32_t block;  // blockIdx.x of the reporter
   uint32_t role;   // warp index inside the CTA
   uint32_t where;  // stage / item index
+};
+
+// A wait that ran out leaves the call's output undefined, a data error only skips
+// accesses: each kind keeps its own first record, so that neither hides the other.
+struct DeviceError {
+  DeviceErrorRecord wait;
+  DeviceErrorRecord data;
 };
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {
@@ -45,10 +52,11 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 
 __device__ __forceinline__ void record_error(DeviceError* err, uint32_t code, uint32_t where) {
   if (err == nullptr) return;
-  if (atomicCAS(&err->code, 0u, code) == 0u) {
-    err->block = blockIdx.x;
-    err->role = threadIdx.x / 32;
-    err->where = where;
+  DeviceErrorRecord* r = code >= kDevFirstDataError ? &err->data : &err->wait;
+  if (atomicCAS(&r->code, 0u, code) == 0u) {
+    r->block = blockIdx.x;
+    r->role = threadIdx.x / 32;
+    r->where = where;
   }
 }
 

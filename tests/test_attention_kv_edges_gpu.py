@@ -139,3 +139,40 @@ def test_a_long_chunk_beside_thousands_of_decode_requests(path):
                                  c.k_scale, c.v_scale)
     bound = 2.0 ** -8 * np.abs(ref) + 2.0 ** (-11 if path == sg.PATH_STREAM else -8) * (W + np.abs(ref)) + 2.0 ** -12 * W
     assert (np.abs(got[rows] - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_a_timeout_is_reported_beside_a_data_error(path):
+    """A bad page id (its keys masked, the output defined) and a copy that never arrives
+    (the output undefined): the caller has to learn of the second, in either order."""
+    lib = sg.load()
+    c = Case([40, 1], [3000, 20], 8, 2, 16)
+    whole = c.run(path=path).clone()
+    clean()
+    keep = int(c.table[1, 0])
+    for first in ("data", "both"):
+        try:
+            c.table[1, 0] = -5
+            if first == "data":  # an earlier launch leaves the data error, a later one times out
+                c.run(path=path)
+                torch.cuda.synchronize()
+                c.table[1, 0] = keep
+            sg.set_wait_timeout_ns(20_000_000)
+            lib.sg_debug_inject_missing_tx(4096)
+            c.run(path=path)
+            st, detail = sg.check_device_errors()
+            assert st == sg.SG_ERR_TIMEOUT and detail[0] in (1, 2, 3, 4), (st, detail)
+        finally:
+            lib.sg_debug_inject_missing_tx(0)
+            sg.set_wait_timeout_ns(2_000_000_000)
+            c.table[1, 0] = keep
+        st, detail = sg.check_device_errors()  # the other record is still there, once
+        assert st == sg.SG_ERR_BAD_INDEX and detail[0] == 17 and detail[3] == 1
+        clean()
+        assert torch.equal(c.run(path=path), whole)
+        clean()
+    c.table[1, 0] = -5  # alone it is still what it was
+    c.run(path=path)
+    st, detail = sg.check_device_errors()
+    assert st == sg.SG_ERR_BAD_INDEX and detail[0] == 17 and detail[3] == 1
+    clean()
