@@ -459,8 +459,14 @@ SG_API int kv_read_nvfp4(const void *cache, int64_t num_pages, int64_t page_pitc
  * it chooses the kernel); rows of Q that belong to no request are not written.
  *
  * Q and O: `tokens` rows of heads * 128 bf16, pitches ldq and ldo.  Scores, softmax
- * and sums are fp32; keys and values enter the products exactly (a code times its
- * scale has at most 6 significant bits).  A value that is NaN reaches only queries
+ * statistics and sums are fp32; keys and values enter the products exactly (a code
+ * times its scale has at most 6 significant bits).  The softmax weights enter the
+ * product with the values rounded: to 11 bits in the streaming kernel, to bf16 (8
+ * bits) in the tcgen05 kernel, whose row sums, as the other's, are of the rounded
+ * weights.  So which kernel a call takes (by all its requests, below) shows in the
+ * last bits; name it where a request must not depend on its neighbours.  The tensor
+ * core's fp32 additions truncate, by about 2^-25 (relative) per 16 keys: below the
+ * weights' rounding up to some 2^21 keys per query in the tcgen05 kernel.  A value that is NaN reaches only queries
  * that see it; a query head with a NaN or an infinity that sees a key gives NaN.
  * Results are the same on every run.
  *
@@ -484,7 +490,10 @@ SG_API int attention_kv_nvfp4(const void *Q, const void *cache, void *O, const i
  * choice), SG_PATH_STREAM (each cache byte read once per 8 or 16 query rows of a kv
  * head; decode steps) or SG_PATH_TENSOR_CORE (tcgen05, up to 256 query rows per
  * decoded key; prefill chunks; heads / kv_heads at most 256).  Any other path:
- * SG_ERR_INVALID_ARG. */
+ * SG_ERR_INVALID_ARG.  SG_PATH_AUTO takes one kernel for the whole call, from what
+ * the host knows: the streaming one if max_q * heads / kv_heads is at most 32, if
+ * tokens * heads / 16 times the block table's width in steps of 64 keys is at most
+ * 2048, or if heads / kv_heads passes 256; else the tcgen05 kernel. */
 SG_API int attention_kv_nvfp4_path(const void *Q, const void *cache, void *O, const int32_t *block_table,
                                    int64_t table_pitch, int64_t max_pages, const int32_t *seq_lens,
                                    const int32_t *cu_q, int64_t batch, int64_t tokens, int64_t max_q, int64_t heads,

@@ -19,7 +19,7 @@
 // whichever CTA of the two arrives last, in a fixed tree.
 //
 // Measured: 8 kv heads of 4 query heads, chunks of 1536 and 511 tokens against 6000 and
-// 511 keys and two decode rows, 160 us (837 TFLOP/s; 229 us with one 128-row tile per
+// 511 keys and two decode rows, 163 us (820 TFLOP/s; 229 us with one 128-row tile per
 // CTA and no equal shares); a chunk of 4096 tokens against 8192 keys, 64 heads, 748 us
 // (1102 TFLOP/s of the 1910 that a large cuBLAS product reaches).  What bounds it is
 // issue latency: a block of 128 keys x 256 rows keeps the tensor core busy for 2176
@@ -39,6 +39,10 @@
 //   warps 20-27   decode: per block each warp one cache tile, K to fp16 and V to bf16,
 //                 exactly, in the 128-byte-swizzled layout the MMA reads (four warps on
 //                 K and four on V wait for the slower V: 198 us against 183)
+// P is rounded to bf16, half a step 2^-8 of a weight, and the row sums are of the rounded
+// weights, so that an average stays one (summing them unrounded: 160 us for the chunks
+// above).  The tensor core's fp32 additions truncate: about 2^-25 per 16 keys that a CTA
+// adds up, 2.3% low at 14 million keys, below P's rounding up to some 2^21.
 // V must be bf16 because P is (weights far below the row maximum count where every
 // larger one meets a zero in V; fp16 would flush them).  E2M1 to bf16 is a shift and
 // a mask: s eem -> s 000000ee m000000 is the value times 2^-126, and the block's
@@ -855,8 +859,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefill_kernel(const KvAttnP
             const uint64_t y = fma_f32x2(xs, scale2, minus2);
             const float p0 = pf_exp2(__uint_as_float(static_cast<uint32_t>(y)));
             const float p1 = pf_exp2(__uint_as_float(static_cast<uint32_t>(y >> 32)));
-            sums[e & 1] = add_f32x2(sums[e & 1], pack_f32x2(p0, p1));
             pk[e] = pf_pack(p0, p1);
+            // (the sum is of the weights that the product takes)
+            sums[e & 1] = add_f32x2(sums[e & 1], pack_f32x2(__uint_as_float(pk[e] << 16),
+                                                            __uint_as_float(pk[e] & 0xFFFF0000u)));
           }
           tmem_st_32x32b_x16(s_col + 32 * half + 16 * c, pk);
         }

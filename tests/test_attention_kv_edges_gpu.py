@@ -176,3 +176,36 @@ def test_a_timeout_is_reported_beside_a_data_error(path):
     st, detail = sg.check_device_errors()
     assert st == sg.SG_ERR_BAD_INDEX and detail[0] == 17 and detail[3] == 1
     clean()
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_constant_value_comes_back(path, causal):
+    """The sums are of the weights as they enter the product, so whatever their rounding
+    the average of one value is that value: fp32 leaves 2^-20 of it, far inside half a
+    step of bf16."""
+    for q_lens, lens in (([1, 1], [700, 90]), ([5], [300]), ([60, 3], [900, 64]), ([200], [1500])):
+        c = Case(q_lens, lens, 8, 2, 16, spread=1.5)
+        k = np.random.default_rng(2).standard_normal((sum(lens), 2, D))
+        fill(c, k=k, v=c.v_scale * np.ones_like(k))
+        got = c.run(causal, path=path)
+        clean()
+        assert (got == ONES * c.v_scale).all(), (got.float() / (ONES * c.v_scale) - 1).abs().max()
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_a_constant_value_under_weights_that_round_alike(path):
+    """256 keys of weight 1, which set the reference, then keys of a weight just past the
+    middle of two bf16 numbers: rounded up, they are 2^-8 too heavy, which shows (half a
+    step at 1.875 is 2^-9) unless the sum takes them the same way."""
+    n = 152  # requests, each about one CTA's share
+    c = Case([1] * n, [1500] * n, 1, 1, 16, v_scale=1.0)
+    k = np.zeros((1500, 1, D))
+    k[:, 0, 0], k[:, 0, 1] = np.where(np.arange(1500) < 256, 4.0, 6.0), 6.0  # held exactly: scale 1
+    fill(c, k=np.tile(k, (n, 1, 1)), v=np.full((n * 1500, 1, D), 1.875))  # scale 5 / 16, code 6
+    q = np.zeros((n, 1, D))
+    q[:, 0, 0] = 16.0
+    c.Q = syn.f64_to_bf16_bits(q)
+    got = c.run(scale=np.log(1 + 2.0 ** -8 + 2.0 ** -11) / 32, path=path)
+    clean()
+    assert (got == 1.875).all(), got.float().unique()
