@@ -20,7 +20,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["sg_api.cu", "sg_gemm_tcgen05.cu", "sg_gemm_nvfp4.cu", "sg_attention.cu", "sg_attention_decode.cu", "sg_gemv_cuda_core.cu", "sg_microbench.cu",
            "sg_noalloc.cu", "sg_kv_cache.cu", "sg_rope.cu", "sg_attention_kv.cu",
            "sg_attention_kv_prefill.cu"]
-HEADERS = ["sg_ptx.cuh", "sg_sched.cuh", "sg_kv.cuh", "sg_internal.h"]
+HEADERS = ["sg_ptx.cuh", "sg_sched.cuh", "sg_kv.cuh", "sg_internal.h", "sg_smem.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",

@@ -533,12 +533,9 @@ cudaError_t launch_attn_combine(const AttnParams& p, cudaStream_t stream) {
 
 cudaError_t launch_attention(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                              const AttnParams& p, cudaStream_t stream) {
-  static bool attr_set = false;
-  if (!attr_set) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAtSmem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static DeviceBits allowed{0};
+  const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(attn_fwd_kernel), kAtSmem, &allowed);
+  if (e != cudaSuccess) return e;
   const int64_t grid = static_cast<int64_t>(p.q_tiles) * p.H * p.B * p.n_splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);

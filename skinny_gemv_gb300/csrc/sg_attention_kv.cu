@@ -1002,13 +1002,9 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) kv_stream_kernel(const K
 template <int NT>
 cudaError_t launch(const KvAttnParams& p, int sms, cudaStream_t stream) {
   using C = Cfg<NT>;
-  static bool attr_set = false;
-  if (!attr_set) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kv_stream_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static DeviceBits allowed{0};
+  const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kv_stream_kernel<NT>), C::kSmem, &allowed);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(sms), 1, 1);
   cfg.blockDim = dim3(C::kThreads, 1, 1);

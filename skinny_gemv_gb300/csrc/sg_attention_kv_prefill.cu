@@ -1036,12 +1036,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefill_kernel(const KvAttnP
 }  // namespace
 
 cudaError_t launch_kv_prefill(const KvAttnParams& p, int ctas, cudaStream_t stream) {
-  static bool attr_set = false;
-  if (!attr_set) {
-    const cudaError_t e = cudaFuncSetAttribute(kv_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPfSmem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static DeviceBits allowed{0};
+  const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kv_prefill_kernel), kPfSmem, &allowed);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
   cfg.blockDim = dim3(kPfThreads, 1, 1);

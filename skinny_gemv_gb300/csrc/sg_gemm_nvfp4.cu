@@ -618,12 +618,9 @@ __global__ void f4_pack_scales_kernel(const uint8_t* __restrict__ plain, int64_t
 }  // namespace
 
 cudaError_t launch_f4_gemm(const CUtensorMap& tmA, const CUtensorMap& tmB, const F4Params& p, cudaStream_t stream) {
-  static bool attr_set = false;
-  if (!attr_set) {
-    const cudaError_t e = cudaFuncSetAttribute(f4_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kF4Smem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static DeviceBits allowed{0};
+  const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(f4_gemm_kernel), kF4Smem, &allowed);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.sched.grid, 1, 1);
   cfg.blockDim = dim3(kF4Threads, 1, 1);
@@ -639,13 +636,9 @@ cudaError_t launch_f4_gemm(const CUtensorMap& tmA, const CUtensorMap& tmB, const
 
 cudaError_t launch_f4_gemm_pair(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmSFA,
                                const CUtensorMap& tmSFB, const F4Params& p, cudaStream_t stream) {
-  static bool attr_set = false;
-  if (!attr_set) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(f4_gemm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kF4PSmem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static DeviceBits allowed{0};
+  const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(f4_gemm_pair_kernel), kF4PSmem, &allowed);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * p.sched.grid, 1, 1);
   cfg.blockDim = dim3(kF4Threads, 1, 1);

@@ -980,12 +980,9 @@ cudaError_t launch_variant(const CUtensorMap& a, const CUtensorMap& b, const CUt
   static const TcBatchMaps kNoBatch{};
   using L = TcLayout<BN, STAGES, SWAP_ROWS, KSUB, PAIR, GATED>;
   auto kern = tc_gemm_kernel<BN, STAGES, SWAP_ROWS, KSUB, PAIR, GATED>;
-  static bool configured = false;  // the attribute is per function, process-wide
-  if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
+  static DeviceBits allowed{0};
+  const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kern), L::kAlloc, &allowed);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((PAIR ? 2 : 1) * p.sched.grid, 1, 1);
   cfg.blockDim = dim3(L::kThreads, 1, 1);

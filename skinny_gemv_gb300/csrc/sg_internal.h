@@ -8,6 +8,7 @@
 
 #include "sg_kv.cuh"
 #include "sg_sched.cuh"
+#include "sg_smem.h"
 
 namespace sg {
 

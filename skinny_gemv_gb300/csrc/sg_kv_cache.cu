@@ -275,13 +275,10 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const KvRowsParams
 
 template <int THREADS>
 cudaError_t launch_pages(const KvPagesParams& p, int grid, cudaStream_t stream) {
-  static bool attr_set = false;
-  if (!attr_set) {
-    const cudaError_t e = cudaFuncSetAttribute(kv_pages_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               2 * sizeof(int32_t) * kKvMaxRequests);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static DeviceBits allowed{0};
+  const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kv_pages_kernel<THREADS>),
+                                           2 * sizeof(int32_t) * kKvMaxRequests, &allowed);
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
       pdl_config(grid, THREADS, 2 * sizeof(int32_t) * static_cast<size_t>(p.requests), stream, attr);

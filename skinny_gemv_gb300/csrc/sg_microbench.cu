@@ -112,12 +112,9 @@ __global__ void __launch_bounds__(512) read_stream_kernel(const uint4* __restric
 
 cudaError_t launch_tc_peak(int64_t iters, int grid, unsigned long long* cycles, unsigned long long* ns,
                            DeviceError* err, cudaStream_t stream) {
-  static bool configured = false;
-  if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(tc_peak_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPeakSmem);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
+  static DeviceBits allowed{0};
+  const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(tc_peak_kernel), kPeakSmem, &allowed);
+  if (e != cudaSuccess) return e;
   tc_peak_kernel<<<grid, 128, kPeakSmem, stream>>>(iters, cycles, ns, err, 4000000000ull);
   return cudaGetLastError();
 }
