@@ -209,3 +209,63 @@ def test_a_constant_value_under_weights_that_round_alike(path):
     got = c.run(scale=np.log(1 + 2.0 ** -8 + 2.0 ** -11) / 32, path=path)
     clean()
     assert (got == 1.875).all(), got.float().unique()
+
+
+@pytest.mark.parametrize("q_lens,lens,heads,kv_heads,page", [
+    ([300], [1500], 8, 2, 16), ([150, 1, 40], [900, 2000, 41], 16, 2, 64), ([513, 0, 2], [513, 7, 1300], 12, 4, 128),
+    ([33] * 20, [33 + 60 * i for i in range(20)], 4, 1, 32), ([1000], [3000], 2, 1, 48)])
+def test_larger_prefill_calls_take_the_tensor_core_kernel(q_lens, lens, heads, kv_heads, page):
+    c = Case(q_lens, lens, heads, kv_heads, page, seed=4)
+    auto, forced = c.run().clone(), c.run(path=sg.PATH_TENSOR_CORE).clone()
+    stream = c.run(path=sg.PATH_STREAM)
+    clean()
+    assert torch.equal(auto, forced) and not torch.equal(auto, stream)
+    check(c, sg.PATH_TENSOR_CORE, auto=True)
+    check(c, sg.PATH_STREAM)
+
+
+@pytest.mark.parametrize("q_lens,lens,heads,kv_heads,page", [
+    ([40], [700], 300, 1, 16),        # too many heads per kv head for the other kernel, 8250 steps
+    ([8, 1], [5000, 3000], 16, 4, 64),   # 32 rows per kv head
+    ([64], [64], 4, 1, 16), ([100, 7], [130, 500], 4, 2, 16)])  # little work
+def test_other_calls_stream(q_lens, lens, heads, kv_heads, page):
+    c = Case(q_lens, lens, heads, kv_heads, page, seed=4)
+    auto, forced = c.run().clone(), c.run(path=sg.PATH_STREAM)
+    clean()
+    assert torch.equal(auto, forced)
+    check(c, sg.PATH_STREAM, auto=True)
+
+
+@pytest.mark.parametrize("q_lens,lens", [([1], [17]), ([2, 3], [700, 64]), ([4, 1, 4], [33, 2000, 129]), ([8], [300]),
+                                         ([16, 5], [257, 1000]), ([70, 9], [400, 9])])
+@pytest.mark.parametrize("heads,kv_heads,page", [(4, 4, 16), (8, 2, 32), (12, 1, 48), (32, 2, 64)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_streaming_weights_keep_eleven_bits(q_lens, lens, heads, kv_heads, page, causal):
+    """Both widths of the streaming kernel (8 and 16 query rows), within the bound of its
+    fp16 weights."""
+    check(Case(q_lens, lens, heads, kv_heads, page, seed=8), sg.PATH_STREAM, causal)
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("below", [20, 30, 60, 90])
+@pytest.mark.parametrize("order", ["heavy first", "light first", "mixed"])
+def test_small_weights_count_where_the_larger_meet_zero(path, below, order):
+    """Keys of two kinds, whose weights differ by 2^below; V is zero under the heavy ones,
+    so the whole result comes from the light ones (and so does W, which the bound is
+    relative to)."""
+    rng = np.random.default_rng(below)
+    for q_lens, lens in (([1], [50]), ([1, 2], [700, 90]), ([6], [400]), ([150], [1000])):
+        c = Case(q_lens, lens, 8, 2, 16, v_scale=1.0)
+        heavy = np.concatenate([np.arange(n) < (n + 1) // 2 if order == "heavy first" else
+                                np.arange(n) >= n // 2 if order == "light first" else rng.random(n) < 0.5 for n in lens])
+        k, v = np.zeros((2, sum(lens), 2, D))
+        k[:, :, 0] = np.where(heavy, 6.0, -6.0)[:, None]  # held exactly: scale 1, code 6
+        v[:] = np.where(heavy[:, None, None], 0.0, rng.standard_normal(v.shape))
+        fill(c, k, v)
+        q = np.zeros((int(c.cu[-1]), 8, D))
+        q[:, :, 0] = 16.0
+        c.Q = syn.f64_to_bf16_bits(q)
+        check(c, path, scale=below * np.log(2.0) / (16 * 12))
+        if order == "heavy first":
+            ref, _ = c.ref(scale=below * np.log(2.0) / (16 * 12))
+            assert 0 < np.abs(ref[-1]).max() < 2.0 ** (4 - below)
