@@ -73,13 +73,6 @@ __device__ __forceinline__ void named_bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// 2^x by the ex2.approx instruction (relative error about 2^-22; 2^-inf = 0).
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
@@ -332,7 +325,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const bool move = mx > m_run + kAtRescaleLog2;
       const float m_new = move ? mx : m_run;
       const float m_use = m_new == -INFINITY ? 0.f : m_new;
-      const float alpha = move ? fast_exp2(m_run - m_use) : 1.f;  // 0 while nothing was visible yet
+      const float alpha = move ? exp2_approx(m_run - m_use) : 1.f;  // 0 while nothing was visible yet
       // weights, rounded to bf16 (the P V product's operand); l sums the rounded
       // values (8 independent partial sums, added in a fixed order)
       uint32_t pk[32];
@@ -343,8 +336,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float p0 = fast_exp2(__uint_as_float(sv[c][2 * e]) - m_use);
-          const float p1 = fast_exp2(__uint_as_float(sv[c][2 * e + 1]) - m_use);
+          const float p0 = exp2_approx(__uint_as_float(sv[c][2 * e]) - m_use);
+          const float p1 = exp2_approx(__uint_as_float(sv[c][2 * e + 1]) - m_use);
           const uint32_t w = pack_bf16x2(p0, p1);
           pk[16 * c + e] = w;
           rs8[e & 7] += bf16_lo(w) + bf16_hi(w);
@@ -480,7 +473,7 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const AttnParams p) {
   float mx = l;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-  const float w = mx == -INFINITY ? 0.f : fast_exp2(l - mx);
+  const float w = mx == -INFINITY ? 0.f : exp2_approx(l - mx);
   float tot = w;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xFFFFFFFFu, tot, o);

@@ -34,12 +34,6 @@ constexpr int kDecWarps = 8;
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kKeysPerStep = kDecWarps * 4;  // keys a CTA takes side by side (key groups x warps)
 
-__device__ __forceinline__ float dec_exp2(float x) {  // 2^x, ex2.approx (2^-inf = 0)
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // 16 bytes of K or V, read once: streamed past L1.
 __device__ __forceinline__ uint4 ld_kv_v4(const uint16_t* p) {
   uint4 v;
@@ -171,14 +165,14 @@ __global__ void __launch_bounds__(kDecThreads, RT >= 4 ? 1 : 2) attn_decode_kern
       for (int c = 1; c < C; ++c) cm = fmaxf(cm, s[r][c]);
       if (cm == -INFINITY) continue;  // nothing visible in this step
       const float mn = fmaxf(m[r], cm);
-      const float corr = dec_exp2(m[r] - mn);  // 0 while nothing was visible
+      const float corr = exp2_approx(m[r] - mn);  // 0 while nothing was visible
       m[r] = mn;
       l[r] *= corr;
 #pragma unroll
       for (int e = 0; e < 16; ++e) o[r][e] *= corr;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const float w = dec_exp2(s[r][c] - mn);
+        const float w = exp2_approx(s[r][c] - mn);
         l[r] += w;
         float vf[16];
         bf16x8_f32(vv[c][0], vf);
@@ -195,7 +189,7 @@ __global__ void __launch_bounds__(kDecThreads, RT >= 4 ? 1 : 2) attn_decode_kern
   for (int r = 0; r < RT; ++r) {
     float mw = fmaxf(m[r], __shfl_xor_sync(0xFFFFFFFFu, m[r], 8));
     mw = fmaxf(mw, __shfl_xor_sync(0xFFFFFFFFu, mw, 16));
-    const float corr = m[r] == -INFINITY ? 0.f : dec_exp2(m[r] - mw);
+    const float corr = m[r] == -INFINITY ? 0.f : exp2_approx(m[r] - mw);
     float lw = l[r] * corr;
     lw += __shfl_xor_sync(0xFFFFFFFFu, lw, 8);
     lw += __shfl_xor_sync(0xFFFFFFFFu, lw, 16);
@@ -228,7 +222,7 @@ __global__ void __launch_bounds__(kDecThreads, RT >= 4 ? 1 : 2) attn_decode_kern
     if (M != -INFINITY) {
 #pragma unroll
       for (int w = 0; w < kDecWarps; ++w) {
-        const float f = sm_m[w][r] == -INFINITY ? 0.f : dec_exp2(sm_m[w][r] - M);
+        const float f = sm_m[w][r] == -INFINITY ? 0.f : exp2_approx(sm_m[w][r] - M);
         L = fmaf(sm_l[w][r], f, L);
         acc = fmaf(sm_o[w][r][d], f, acc);
       }

@@ -94,12 +94,6 @@ struct Cfg {
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
-__device__ __forceinline__ float kv_exp2(float x) {  // 2^x, ex2.approx (2^-inf = 0)
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Shared-memory loads by 32-bit address (volatile: the bytes are written by copies).
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -160,8 +154,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
-
 __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -177,18 +169,6 @@ __device__ __forceinline__ void tile_load(uint32_t dst, const uint8_t* src, uint
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(reinterpret_cast<uint64_t>(src)), "n"(kKvTileBytes), "r"(bar)
                : "memory");
-}
-
-// The four code pairs of a word as fp16 pairs, times a scale (exact).
-__device__ __forceinline__ void decode4(uint32_t w, __half2 s, uint32_t (&o)[4]) {
-  uint32_t c[4];
-  asm("{\n\t.reg .b8 t, u, v, w;\n\tmov.b32 {t, u, v, w}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, t;\n\tcvt.rn.f16x2.e2m1x2 %1, u;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, v;\n\tcvt.rn.f16x2.e2m1x2 %3, w;\n\t}"
-      : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
-      : "r"(w));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = half2_bits(__hmul2(*reinterpret_cast<const __half2*>(&c[i]), s));
 }
 
 // Scores of two tiles (32 keys) at shared address `st`: s[tile][nt] holds keys g8 (0, 1)
@@ -215,8 +195,8 @@ __device__ __forceinline__ void scores(uint32_t st, int lane, const uint32_t (&q
       const uint32_t wa = i == 0 ? k[tl][0].x : i == 1 ? k[tl][0].y : i == 2 ? k[tl][0].z : k[tl][0].w;
       const uint32_t wb = i == 0 ? k[tl][1].x : i == 1 ? k[tl][1].y : i == 2 ? k[tl][1].z : k[tl][1].w;
       uint32_t a[4], b[4];
-      decode4(wa, i < 2 ? __low2half2(sa) : __high2half2(sa), a);
-      decode4(wb, i < 2 ? __low2half2(sb) : __high2half2(sb), b);
+      e2m1x8_times(wa, i < 2 ? __low2half2(sa) : __high2half2(sa), a);
+      e2m1x8_times(wb, i < 2 ? __low2half2(sb) : __high2half2(sb), b);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         mma_f16(s[tl][nt], a[0], b[0], a[1], b[1], qf[nt][4 * i], qf[nt][4 * i + 1]);
@@ -243,7 +223,7 @@ __device__ __forceinline__ void values(uint32_t tile, uint32_t sc, int lane, con
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float u = kv_exp2(d[nt][2 * h]), v = kv_exp2(d[nt][2 * h + 1]);
+      float u = exp2_approx(d[nt][2 * h]), v = exp2_approx(d[nt][2 * h + 1]);
       if (W == Weights::kWide) {
         const uint32_t tu = to_tf32(u), tv = to_tf32(v);
         const uint32_t lo = transpose8x8(__byte_perm(tu, tv, 0x5410)), hi = transpose8x8(__byte_perm(tu, tv, 0x7632));
@@ -268,10 +248,10 @@ __device__ __forceinline__ void values(uint32_t tile, uint32_t sc, int lane, con
   for (int h = 0; h < 2; ++h) {
     const uint32_t a = h ? va.y : va.x, b = h ? va.w : va.z, c = h ? vb.y : vb.x, e = h ? vb.w : vb.z;
     uint32_t a0[4], a1[4], a2[4], a3[4];
-    decode4((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), s0, a0);
-    decode4(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), s0, a1);
-    decode4((c & 0x0F0F0F0Fu) | ((e << 4) & 0xF0F0F0F0u), s1, a2);
-    decode4(((c >> 4) & 0x0F0F0F0Fu) | (e & 0xF0F0F0F0u), s1, a3);
+    e2m1x8_times((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), s0, a0);
+    e2m1x8_times(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), s0, a1);
+    e2m1x8_times((c & 0x0F0F0F0Fu) | ((e << 4) & 0xF0F0F0F0u), s1, a2);
+    e2m1x8_times(((c >> 4) & 0x0F0F0F0Fu) | (e & 0xF0F0F0F0u), s1, a3);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -669,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) kv_stream_kernel(const K
                   mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16)) * col_scale[nt][c];
                   if (mx - ref[nt][c] > kMoveAbove) {
                     const float next = mx - kRefShift;
-                    const float f = kv_exp2(ref[nt][c] - next);
+                    const float f = exp2_approx(ref[nt][c] - next);
                     ref[nt][c] = next;
                     l[nt][c] *= f;
                     l[nt][c + 2] *= f;
@@ -837,7 +817,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) kv_stream_kernel(const K
     float top = m;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    f = kv_exp2(m - top);
+    f = exp2_approx(m - top);
     sum = l * f;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
@@ -941,7 +921,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) kv_stream_kernel(const K
         float f, part_sum;
         const float part_top = join(ms.x, ms.y, f, part_sum);
         const float now = fmaxf(top, part_top);
-        const float keep = kv_exp2(top - now), add = kv_exp2(part_top - now);
+        const float keep = exp2_approx(top - now), add = exp2_approx(part_top - now);
         top = now;
         sum = sum * keep + part_sum * add;
         acc.x *= keep;
@@ -1005,16 +985,8 @@ cudaError_t launch(const KvAttnParams& p, int sms, cudaStream_t stream) {
   static DeviceBits allowed{0};
   const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kv_stream_kernel<NT>), C::kSmem, &allowed);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(sms), 1, 1);
-  cfg.blockDim = dim3(C::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  const cudaLaunchConfig_t cfg = pdl_config(sms, C::kThreads, C::kSmem, stream, attr);
   return cudaLaunchKernelEx(&cfg, kv_stream_kernel<NT>, p);
 }
 

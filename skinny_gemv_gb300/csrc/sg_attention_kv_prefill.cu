@@ -143,32 +143,12 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-__device__ __forceinline__ float pf_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t pf_pack(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ void pf_bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-// Four pairs of E2M1 codes (bytes) to fp16 pairs times a scale (exact).
-__device__ __forceinline__ uint4 k_decode(uint32_t w, __half2 s) {
-  uint32_t c[4];
-  asm("{\n\t.reg .b8 t, u, v, w;\n\tmov.b32 {t, u, v, w}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, t;\n\tcvt.rn.f16x2.e2m1x2 %1, u;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, v;\n\tcvt.rn.f16x2.e2m1x2 %3, w;\n\t}"
-      : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
-      : "r"(w));
-  return make_uint4(h2_bits(__hmul2(*reinterpret_cast<__half2*>(&c[0]), s)),
-                    h2_bits(__hmul2(*reinterpret_cast<__half2*>(&c[1]), s)),
-                    h2_bits(__hmul2(*reinterpret_cast<__half2*>(&c[2]), s)),
-                    h2_bits(__hmul2(*reinterpret_cast<__half2*>(&c[3]), s)));
 }
 
 // Eight E2M1 codes of a word to bf16 times scale * 2^-16, in the order 0, 4, 1, 5, 2,
@@ -670,8 +650,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefill_kernel(const KvAttnP
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   const int chunk = 4 * (t4 & 1) + (k ^ (flip ? 2 : 0));
-                  *reinterpret_cast<uint4*>(box + r * 128 + ((chunk ^ (r & 7)) * 16)) =
-                      k_decode(w[k], k < 2 ? __low2half2(sf) : __high2half2(sf));
+                  uint32_t o[4];
+                  e2m1x8_times(w[k], k < 2 ? __low2half2(sf) : __high2half2(sf), o);
+                  *reinterpret_cast<uint4*>(box + r * 128 + ((chunk ^ (r & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
               }
             }
@@ -754,9 +735,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefill_kernel(const KvAttnP
           // or an infinity becomes NaN as a whole, as its softmax is (infinite scores of one
           // sign would all be -inf and pass for masked keys)
           const float up = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : __int_as_float((127 + 13 - e) << 23) * sign;
-          const uint32_t lo = h2_bits(
+          const uint32_t lo = half2_bits(
               __floats2half2_rn(__uint_as_float(v[i].x << 16) * up, __uint_as_float(v[i].x & 0xFFFF0000u) * up));
-          const uint32_t hi = h2_bits(
+          const uint32_t hi = half2_bits(
               __floats2half2_rn(__uint_as_float(v[i].y << 16) * up, __uint_as_float(v[i].y & 0xFFFF0000u) * up));
           const int chunk = (lane / 2) & 7;
           uint8_t* box = smem + kPfQOff + (2 * (r / kPfTileRows) + lane / 16) * kPfBox + (r % kPfTileRows) * 128;
@@ -834,7 +815,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefill_kernel(const KvAttnP
         const bool move = mx > m_run + kPfRescaleLog2;
         const float m_new = move ? mx : m_run;
         const float m_use = m_new == -INFINITY ? 0.f : m_new;
-        const float alpha = move ? pf_exp2(m_run - m_use) : 1.f;  // 0 while nothing was visible yet
+        const float alpha = move ? exp2_approx(m_run - m_use) : 1.f;  // 0 while nothing was visible yet
         m_run = m_new;
         // (S of this block is there, so the product of the last one is done with O)
         if (i > 0 && __any_sync(0xFFFFFFFFu, move)) {
@@ -857,8 +838,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefill_kernel(const KvAttnP
           for (int e = 0; e < 16; ++e) {
             const uint64_t xs = pack_f32x2(__uint_as_float(sv[c][2 * e]), __uint_as_float(sv[c][2 * e + 1]));
             const uint64_t y = fma_f32x2(xs, scale2, minus2);
-            const float p0 = pf_exp2(__uint_as_float(static_cast<uint32_t>(y)));
-            const float p1 = pf_exp2(__uint_as_float(static_cast<uint32_t>(y >> 32)));
+            const float p0 = exp2_approx(__uint_as_float(static_cast<uint32_t>(y)));
+            const float p1 = exp2_approx(__uint_as_float(static_cast<uint32_t>(y >> 32)));
             pk[e] = pf_pack(p0, p1);
             // (the sum is of the weights that the product takes)
             sums[e & 1] = add_f32x2(sums[e & 1], pack_f32x2(__uint_as_float(pk[e] << 16),
@@ -908,8 +889,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefill_kernel(const KvAttnP
         if (x == 0) {
           const float2 ml = *reinterpret_cast<const float2*>(swap + kKvDim);
           const float top = fmaxf(m_run, ml.x), use = top == -INFINITY ? 0.f : top;
-          mine_f = pf_exp2(m_run - use);
-          other_f = pf_exp2(ml.x - use);
+          mine_f = exp2_approx(m_run - use);
+          other_f = exp2_approx(ml.x - use);
           l_run = l_run * mine_f + ml.y * other_f;
           m_run = top;
         }
@@ -1009,7 +990,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefill_kernel(const KvAttnP
               const int row = row0 + kWarps * k;
               if (row >= cur->rows) break;
               const float top = fmaxf(ma[k].x, mb[k].x);
-              const float fa = pf_exp2(ma[k].x - top), fb = pf_exp2(mb[k].x - top);
+              const float fa = exp2_approx(ma[k].x - top), fb = exp2_approx(mb[k].x - top);
               const float sum = ma[k].y * fa + mb[k].y * fb;
               const float4 o = make_float4(va[k].x * fa + vb[k].x * fb, va[k].y * fa + vb[k].y * fb,
                                            va[k].z * fa + vb[k].z * fb, va[k].w * fa + vb[k].w * fb);
@@ -1039,16 +1020,8 @@ cudaError_t launch_kv_prefill(const KvAttnParams& p, int ctas, cudaStream_t stre
   static DeviceBits allowed{0};
   const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kv_prefill_kernel), kPfSmem, &allowed);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
-  cfg.blockDim = dim3(kPfThreads, 1, 1);
-  cfg.dynamicSmemBytes = kPfSmem;
-  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  const cudaLaunchConfig_t cfg = pdl_config(ctas, kPfThreads, kPfSmem, stream, attr);
   return cudaLaunchKernelEx(&cfg, kv_prefill_kernel, p);
 }
 

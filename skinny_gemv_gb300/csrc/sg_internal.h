@@ -250,6 +250,22 @@ cudaError_t launch_attention(const CUtensorMap& tmQ, const CUtensorMap& tmK, con
                              const AttnParams& p, cudaStream_t stream);
 
 // ------------------------------------------------- paged NVFP4 KV cache, rotation
+// A one-dimensional launch that may begin before the kernel ahead of it has ended (it
+// waits for it itself); `attr` is one attribute that outlives the launch.
+inline cudaLaunchConfig_t pdl_config(int64_t grid, int threads, size_t smem, cudaStream_t stream,
+                                     cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
 constexpr int kKvMaxRequests = 16384;  // two int32 per request in a CTA's shared memory
 
 struct KvPagesParams {

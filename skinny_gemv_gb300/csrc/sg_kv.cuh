@@ -67,6 +67,21 @@ __device__ __forceinline__ __half2 e2m1x2_half2(uint32_t byte) {
   return *reinterpret_cast<const __half2*>(&r);
 }
 
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+
+// Eight E2M1 codes (a word, low nibble first) to four half2 times a scale (exact: 2 + 4
+// significant bits).
+__device__ __forceinline__ void e2m1x8_times(uint32_t w, __half2 s, uint32_t (&o)[4]) {
+  uint32_t c[4];
+  asm("{\n\t.reg .b8 t, u, v, w;\n\tmov.b32 {t, u, v, w}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, t;\n\tcvt.rn.f16x2.e2m1x2 %1, u;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, v;\n\tcvt.rn.f16x2.e2m1x2 %3, w;\n\t}"
+      : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = half2_bits(__hmul2(*reinterpret_cast<const __half2*>(&c[i]), s));
+}
+
 // Eight floats to a word of E2M1 codes, the first in the low nibble (nearest, ties to
 // even, magnitudes past 6 to 6).
 __device__ __forceinline__ uint32_t e2m1x8_from(const float (&y)[8]) {

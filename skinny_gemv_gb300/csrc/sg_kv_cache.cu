@@ -12,19 +12,6 @@
 namespace sg {
 namespace {
 
-cudaLaunchConfig_t pdl_config(int64_t grid, int threads, size_t smem, cudaStream_t stream, cudaLaunchAttribute* attr) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cfg;
-}
-
 // ------------------------------------------------------------ page assignment
 // Inclusive block scan (sum) over THREADS threads; `warp_sums` is scratch of 32
 // values.  Ends with a barrier, so the scratch may be reused at once.

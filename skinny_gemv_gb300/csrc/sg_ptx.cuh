@@ -44,6 +44,13 @@ struct DeviceError {
   DeviceErrorRecord data;
 };
 
+// 2^x by ex2.approx (relative error about 2^-22; 2^-inf = 0, results below 2^-126 are 0).
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ uint64_t globaltimer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));

@@ -157,15 +157,9 @@ cudaError_t launch_rows(RopeParams p, cudaStream_t stream) {
   constexpr int kRowsPerWarp = 32 / LPR * R;
   p.items_per_token = (p.heads + p.kv_heads + kRowsPerWarp - 1) / kRowsPerWarp;
   const int64_t items = static_cast<int64_t>(p.tokens) * p.items_per_token;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((items + kRopeThreads / 32 - 1) / (kRopeThreads / 32)), 1, 1);
-  cfg.blockDim = dim3(kRopeThreads, 1, 1);
-  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  const cudaLaunchConfig_t cfg =
+      pdl_config((items + kRopeThreads / 32 - 1) / (kRopeThreads / 32), kRopeThreads, 0, stream, attr);
   return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<LPR, R>, p);
 }
 
