@@ -376,13 +376,15 @@ SG_API int64_t kv_nvfp4_page_bytes(int64_t kv_heads, int64_t page_size);
  *
  * total_lens[b] = len + new, *free_head_out = *free_head + pages taken.  A request
  * that does not fit as a whole (its table row, the `tokens` rows of slots and
- * positions, or the free pages left after the requests before it) or whose lengths
- * are negative gets nothing: slots -1, positions 0, total_lens[b] = len; *unserved
- * counts such requests.  Rows past cu_new[requests] (padding of a captured step)
+ * positions, or the free pages) or whose lengths are negative gets nothing: slots
+ * -1, positions 0, total_lens[b] = len; *unserved counts such requests.  Pages are
+ * granted in order: from the first request that the free list cannot serve on, only
+ * requests that need no page are.  Rows past cu_new[requests] (padding of a captured step)
  * get slot -1, position 0.
  *
  * total_lens may be seq_lens and free_head_out may be free_head (a captured step
- * that advances itself); the other arrays must not overlap.  Errors:
+ * that advances itself; one CTA then does the whole step, which a prompt of many
+ * thousand tokens feels); the other arrays must not overlap.  Errors:
  * SG_ERR_INVALID_ARG, SG_ERR_MISALIGNED (4-byte alignment),
  * SG_ERR_UNSUPPORTED_DEVICE, SG_ERR_CUDA; SG_ERR_BAD_INDEX later for a page id
  * that is negative or whose slots pass 2^31 (that row gets slot -1).
@@ -466,9 +468,9 @@ SG_API int kv_read_nvfp4(const void *cache, int64_t num_pages, int64_t page_pitc
  * weights.  So which kernel a call takes (by all its requests, below) shows in the
  * last bits; name it where a request must not depend on its neighbours.  The tensor
  * core's fp32 additions truncate, by about 2^-25 (relative) per 16 keys: below the
- * weights' rounding up to some 2^21 keys per query in the tcgen05 kernel.  A value that is NaN reaches only queries
- * that see it; a query head with a NaN or an infinity that sees a key gives NaN.
- * Results are the same on every run.
+ * weights' rounding up to some 2^21 keys per query in the tcgen05 kernel.  A value
+ * that is NaN reaches only queries that see it; a query head with a NaN or an
+ * infinity that sees a key gives NaN.  Results are the same on every run.
  *
  * A request whose lengths contradict the call (negative, more than max_q queries,
  * more keys than max_pages * page_size, rows outside [0, tokens)) is not computed,

@@ -884,14 +884,18 @@ KvCache kv_cache(void* cache, int64_t num_pages, int64_t page_pitch, int64_t pag
 }
 
 // attention_kv_nvfp4's kernel for `rows` query rows per kv head of the longest request
-// and at most `steps` pieces of 16 rows x 64 keys in all (by the widest block table row).
-// Measured (us, stream / tcgen05), 16 requests of 4096 keys, 32 heads on 8: 24 rows
-// 60.5 / 66.5, 32 rows 62.9 / 64.0, 40 rows 80.9 / 64.7, 64 rows 100.6 / 64.5; 64
-// requests of 1000 keys: 32 rows 70.6 / 87.0, 48 rows 95.5 / 87.5; one of 65536: 32 rows
-// 63.8 / 71.5, 64 rows 96.6 / 71.6.  Few steps, where the tcgen05 kernel's units last
-// longer than the stream: one request of 64 tokens and keys (128 steps) 10.9 / 27.7, two
-// of 16 tokens and 1000 keys (1024) 16.1 / 28.9, one of 64 and 4096, 8 heads (2048)
-// 25.8 / 34.1, but 16 of 12 and 500 (half as many again) 31.1 / 18.3.
+// and at most `steps` pieces of 16 rows x 64 keys in all.  The host knows no lengths, so
+// `steps` takes every request as long as the block table is wide: a small call with a
+// table for long ones goes to the tcgen05 kernel (64 tokens and keys, a table for 131072:
+// 28 us instead of 11).
+// Measured (us, stream / tcgen05, tables as wide as the longest request), 32 heads on 8:
+// 16 requests of 4096 keys, 24 rows 58.2 / 69.1, 32 rows 59.9 / 66.0, 40 rows 78.2 / 66.8,
+// 64 rows 97.7 / 66.9; 64 requests of 1000 keys, 32 rows 67.5 / 89.4, 48 rows 93.1 / 90.4;
+// one of 65536, 32 rows 61.6 / 73.4, 64 rows 93.4 / 74.2.  Few steps, where the tcgen05
+// kernel's units last longer than the stream: one request of 64 tokens and keys (128
+// steps) 10.9 / 28.2, two of 16 tokens and 1000 keys (1024) 16.0 / 28.5, one of 64 and
+// 4096, 8 heads on 2 (2048) 25.5 / 51.6, but 16 of 12 and 500 (half as many again)
+// 30.2 / 17.8.
 int kv_attention_path(int64_t rows, int64_t group, int64_t steps) {
   return rows <= 32 || steps <= 2048 || group > kKvPrefillRows ? SG_PATH_STREAM : SG_PATH_TENSOR_CORE;
 }
@@ -1242,7 +1246,9 @@ int kv_pages_assign(const int32_t* seq_lens, const int32_t* new_lens, int64_t re
   p.free_head_out = free_head_out;
   p.unserved = unserved;
   p.err = d->err;
-  // In place (an output over its input), one CTA: it has read every input before it
+  // In place (an output over its input), one CTA, whatever the size (257 requests with a
+  // million tokens 611 us against 10.2 with outputs of its own; a decode step is one CTA
+  // either way): it has read every input before it
   // writes.  Else a CTA per kPagesRowsPerCta token rows, at most one per SM.
   const bool in_place = total_lens == seq_lens || free_head_out == free_head;
   const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(ceil_div(tokens, kPagesRowsPerCta), d->sm_count));

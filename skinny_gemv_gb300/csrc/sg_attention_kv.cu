@@ -27,7 +27,7 @@
 // of the largest) are normal fp16 numbers, one rounding of 2^-11 each.  Smaller weights
 // count where every larger one meets a zero in V: a step that holds some down to 2^-38
 // takes a second product of those, times 2^24; with smaller ones still, its value
-// product runs on m16n8k8 tf32 (2^-12, fp32's exponents).
+// product runs on m16n8k8 tf32 (11 bits as well, fp32's exponents).
 // The sums use the rounded weights.  Sums and the merges are fp32.
 //
 // Schedule.  A step is 32 NT keys.  The units' steps laid end to end are cut into
@@ -47,6 +47,9 @@
 // MB, 54 us (3.9 TB/s).  The loop itself runs at 5.9 TB/s, bound by issue (ALU pipe 46%,
 // issue slots 50% of active cycles: 306 instructions per 2304-byte tile and warp); the
 // plan and first loads take 7 us and the merges and the tail of uneven warps up to 10.
+// One query against 4096 keys, 32 heads with their own: 19.4 us, most of it plan, first
+// loads and merges (runs per CTA instead of per warp took 15 there, but 83 and 66 on the
+// two above).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

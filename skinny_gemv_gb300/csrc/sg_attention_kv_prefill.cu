@@ -20,8 +20,8 @@
 //
 // Measured: 8 kv heads of 4 query heads, chunks of 1536 and 511 tokens against 6000 and
 // 511 keys and two decode rows, 163 us (820 TFLOP/s; 229 us with one 128-row tile per
-// CTA and no equal shares); a chunk of 4096 tokens against 8192 keys, 64 heads, 748 us
-// (1102 TFLOP/s of the 1910 that a large cuBLAS product reaches).  What bounds it is
+// CTA and no equal shares); a chunk of 4096 tokens against 8192 keys, 64 heads on 8, 762
+// us (1083 TFLOP/s of the 1967 that a large cuBLAS product reaches).  What bounds it is
 // issue latency: a block of 128 keys x 256 rows keeps the tensor core busy for 2176
 // clocks of some 3800; its issuing warp's waits and the softmax (1600 clocks a tile,
 // twice per block, overlapped) take the rest, and a unit's start and end some 10 us.
@@ -951,7 +951,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefill_kernel(const KvAttnP
       if (cur->nblk < cur->unit_blocks) {
         // Cut unit: its pieces' parts are merged two by two, in a tree over the pieces in
         // order; of two neighbours the one that arrives last merges both (64 tokens against
-        // 65536 keys, 19 pieces a unit: 141 us with one CTA merging them all, 115 so).
+        // 65536 keys, 19 pieces a unit: 118 us; with one CTA merging them all 26 more).
         const int64_t piece0 = cur->unit_at / share;
         const int pieces = static_cast<int>((cur->unit_at + cur->unit_blocks - 1) / share - piece0 + 1);
         int first = static_cast<int>(blockIdx.x - piece0);  // of the pieces merged here so far

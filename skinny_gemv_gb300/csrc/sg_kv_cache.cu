@@ -52,7 +52,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums) {
 // A small step (a decode batch) is one CTA of 128 threads: barriers of 32 warps cost
 // it 1 us.  All positions fit 31 bits (total_lens is int32), so divisions are 32-bit.
 // Bound by latency (two scans, then one dependent read and the stores): measured 5.2 us
-// for 64 requests, 9.7 us for 257 requests with a million new tokens (8.5 MB).
+// for 64 requests, 10.2 us for 257 requests with a million new tokens (8.5 MB).
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) kv_pages_kernel(const KvPagesParams p) {
   extern __shared__ int32_t smem[];
@@ -190,7 +190,9 @@ __device__ __forceinline__ bool kv_place(const KvRowsParams& p, uint32_t t, uint
 // halves of a row's sectors took separate passes through L1).
 // Bound by memory; a token's 144 bytes per head lie in four places of its tile, two of
 // them single bytes for the scales.  Measured: 8191 tokens x 8 heads appended and read
-// back, 77 MB in two launches, 21.9 us (3.5 TB/s); 64 tokens 3.5 us for the two.
+// back, 77 MB in two launches, 22.1 us (3.5 TB/s); 64 tokens 3.5 us for the two.  Apart,
+// 38 MB each: append 11.8 us with slots consecutive inside pages and 12.7 scattered, read
+// 10.9 and 11.3; a plain device copy of 38 MB took 14.3.
 constexpr int kRowLanes = kKvDim / 8;
 
 // Splits a thread index into (token, kv head, lane of the row); false past the end.
